@@ -51,6 +51,16 @@ fp8q_status check_grouped_sizes(uint32_t tokens, uint32_t total, uint32_t expert
     return FP8Q_OK;
 }
 
+// The plan and both projections of the FFN.
+fp8q_status check_moe_sizes(uint32_t tokens, uint32_t topk, uint32_t experts, uint32_t d, uint32_t i) {
+    fp8q_status st = check_route_sizes(tokens, topk, experts);
+    if (st != FP8Q_OK) return st;
+    if (i >= kLimit / 2) return FP8Q_ERR_SHAPE;
+    const uint32_t slots = tokens * topk;
+    if ((st = check_grouped_sizes(tokens, slots, experts, 2 * i, d)) != FP8Q_OK) return st;
+    return check_grouped_sizes(slots, slots, experts, d, i);
+}
+
 // Offsets of the grouped projection's workspace: codes, scales, counters, partials, end.
 void grouped_layout(uint32_t total, uint32_t experts, uint32_t k, size_t (&off)[5]) {
     off[0] = 0;
@@ -174,7 +184,7 @@ fp8q_status fp8q_grouped_linear(const void* x, const int32_t* offsets, const int
 }
 
 size_t fp8q_moe_ffn_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t experts, uint32_t d, uint32_t i) {
-    if (check_route_sizes(tokens, topk, experts) != FP8Q_OK || bad_dim(d) || bad_dim(i)) return 0;
+    if (check_moe_sizes(tokens, topk, experts, d, i) != FP8Q_OK) return 0;
     return moe_layout(tokens, topk, experts, d, i).total;
 }
 
@@ -183,12 +193,9 @@ fp8q_status fp8q_moe_ffn(const void* x, const int32_t* topk_ids, const float* to
                          int32_t weight_format, void* y, void* workspace, size_t workspace_bytes, uint32_t tokens,
                          uint32_t topk, uint32_t experts, uint32_t d, uint32_t i, void* stream) {
     if (bad_format(weight_format)) return FP8Q_ERR_ARG;
-    fp8q_status st = check_route_sizes(tokens, topk, experts);
+    fp8q_status st = check_moe_sizes(tokens, topk, experts, d, i);
     if (st != FP8Q_OK) return st;
-    if (bad_dim(d) || bad_dim(i) || i >= kLimit / 2) return FP8Q_ERR_SHAPE;
     const uint32_t slots = tokens * topk;
-    if ((st = check_grouped_sizes(tokens, slots, experts, 2 * i, d)) != FP8Q_OK) return st;
-    if ((st = check_grouped_sizes(slots, slots, experts, d, i)) != FP8Q_OK) return st;
     if (tokens == 0) return FP8Q_OK;
     if (!x || !topk_ids || !topk_weights || !w_gate_up || !w_gate_up_scale || !w_down || !w_down_scale || !y || !workspace)
         return FP8Q_ERR_NULL;

@@ -97,6 +97,26 @@ def test_moe_sizes(change):
     assert call("fp8q_moe_ffn", **change) == SHAPE
 
 
+@pytest.mark.parametrize("change", [dict(d=100), dict(i=0), dict(i=192), dict(i=1 << 31), dict(i=1 << 30), dict(experts=0), dict(experts=MAX_EXPERTS + 1),
+                                    dict(topk=0), dict(topk=MAX_TOPK + 1), dict(tokens=1 << 22), dict(tokens=1 << 30),
+                                    dict(tokens=1 << 20, d=1024, i=128), dict(tokens=1 << 20, i=1024), dict(d=1 << 20, i=1 << 10),
+                                    dict(experts=256, d=1 << 23), dict(experts=256, d=128, i=1 << 22)])
+def test_moe_workspace_of_refused_sizes_is_zero(change):
+    """The workspace query and the call refuse the same sizes: a program that asks first never allocates for a call that will not run."""
+    assert call("fp8q_moe_ffn", **change) == SHAPE
+    a = {**DEFAULTS["fp8q_moe_ffn"], **change}
+    assert api.moe_ffn_workspace_bytes(a["tokens"], a["topk"], a["experts"], a["d"], a["i"]) == 0
+
+
+def test_moe_workspace_of_the_largest_sizes():
+    """Just inside the limits the query answers, and so does the call."""
+    for change in (dict(tokens=(1 << 20) - 1, topk=2, d=1024, i=128), dict(experts=MAX_EXPERTS, tokens=1, topk=MAX_TOPK)):
+        a = {**DEFAULTS["fp8q_moe_ffn"], **change}
+        need = api.moe_ffn_workspace_bytes(a["tokens"], a["topk"], a["experts"], a["d"], a["i"])
+        assert need > 0
+        assert call("fp8q_moe_ffn", **change, bytes=need - 1) == WORKSPACE
+
+
 @pytest.mark.parametrize("change", [dict(n=0), dict(n=100), dict(k=192), dict(rank=0), dict(rank=12), dict(rank=MAX_RANK + 8), dict(adapters=0),
                                     dict(adapters=1 << 23), dict(m=1 << 23), dict(n=1 << 20, k=1 << 11)])
 def test_lora_sizes(change):
