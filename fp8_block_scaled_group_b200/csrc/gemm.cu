@@ -1076,15 +1076,20 @@ cudaError_t read_clear_device_error(uint32_t* code, cudaStream_t stream) {
     return e;
 }
 
+// Once per device ordinal: the attribute is the device's.
 template <uint32_t NT, bool FUSE, bool LORA>
 cudaError_t decode_smem_optin() {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(gemm_decode_kernel<NT, FUSE, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(decode_smem_bytes<NT>()));
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        err[dev] = cudaFuncSetAttribute(gemm_decode_kernel<NT, FUSE, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(decode_smem_bytes<NT>()));
     });
-    return err;
+    return err[dev];
 }
 
 // K split for `slices` weight slices of G K blocks: about 1.6 CTAs per SM
