@@ -111,20 +111,22 @@ fp8q_status check_lora_sizes(uint32_t m, uint32_t n, uint32_t k, uint32_t adapte
 // Whether the decode kernel runs the projection with adapters, 64 rows at a time:
 // always for a decode batch, and up to 256 rows while its second sum, m n rank
 // products on the CUDA cores, is small. The pair kernel multiplies every adapter of
-// 256 rows with all of them. Decode against pair kernel, us at N = 6144, K = 5120: 128
-// rows, 64 adapters of rank 16, 66 and 109; one adapter, 28 and 31; of rank 64, 122
-// and 103; 256 rows, 8 adapters of rank 16, 58 and 38; at N = 1792, K = 4224, 24 and 33.
+// 256 rows with all of them, 32 of the rank at a time. How many adapters the rows use
+// decides as well, but only the device knows it. Decode against pair kernel, us at
+// N = 6144, K = 5120: 128 rows, one adapter of rank 16, 28 and 32; 8 of them, 36 and 42;
+// 64, 65 and 98; one of rank 64, 43 and 33; 8, 77 and 51; 64, 122 and 135; 256 rows, 8
+// adapters of rank 16, 57 and 44; 64, 104 and 120; at N = 1792, K = 4224, 8, 25 and 34.
 bool lora_decode(uint32_t m, uint32_t n, uint32_t rank) {
     if (m <= kDecodeMaxTokens) return true;
     return m <= 256 && static_cast<uint64_t>(m) * n <= 1200000u && static_cast<uint64_t>(rank) * n <= 200000u;
 }
 
-// Offsets of the adapters' workspace: codes, K-major scales, v, lists of adapters, end.
+// Offsets of the adapters' workspace: codes, K-major scales, v (room for either form), lists of adapters, end.
 void lora_layout(uint32_t m, uint32_t k, uint32_t rank, size_t (&off)[5]) {
     off[0] = 0;
     off[1] = off[0] + round_up(static_cast<size_t>(m) * k);
     off[2] = off[1] + round_up(static_cast<size_t>(fp8q_m_pad(m)) * (k / kGroup) * sizeof(float));
-    off[3] = off[2] + round_up(static_cast<size_t>(m) * rank * sizeof(float));
+    off[3] = off[2] + round_up(static_cast<size_t>(m) * v_parts(rank) * sizeof(uint16_t));
     off[4] = off[3] + round_up((static_cast<size_t>(m) + 255) / 256 * kAdapterList * sizeof(int32_t));
 }
 

@@ -150,8 +150,9 @@ __device__ __forceinline__ void spin_cycles(long long cycles) {
 constexpr uint32_t kDirectScalesMaxG = 64;
 
 // kLora: after the G blocks of K a tile has, for each adapter a that its 256
-// rows use, ceil(rank/64) more blocks, bf16 instead of e4m3: v[t] (the row's
-// scaled A_a x, [M, rank]) times B_a[c]. A block is 128 bytes of each operand
+// rows use, ceil(rank/32) more blocks, bf16 instead of e4m3: v[t] (the row's
+// scaled A_a x in two bf16 parts, as v_parts says) times B_a[c], both parts with the
+// same columns of B. A block is 128 bytes of each operand
 // row either way, so the stages and the TMEM buffers serve both; the
 // promotion adds such a block to the rows whose adapter it is, and warps
 // without such a row skip it. The output is rounded once.
@@ -205,8 +206,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const uint32_t G = sh.G;
-    // Adapter blocks: 64 of the rank each; the tile's list of adapters.
-    const uint32_t per_adapter = kLora ? (lo.rank + 63u) / 64u : 0u;
+    // Adapter blocks: 32 of the rank each; the tile's list of adapters.
+    const uint32_t per_adapter = kLora ? (lo.rank + 31u) / 32u : 0u;
     auto list_of = [&](uint32_t m0) { return lo.lists + static_cast<size_t>(m0 / BM_PAIR) * kAdapterList; };
 
     uint32_t issued = 0;  // producer: K blocks whose loads were issued (all tiles)
@@ -240,9 +241,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (kb >= G) {
                             const uint32_t full_even = mapa_shared(smem_addr(&sm.full[s]), 0);
                             const uint32_t a = (kb - G) / per_adapter;
-                            const int32_t r0 = static_cast<int32_t>((kb - G - a * per_adapter) * 64u);
+                            const int32_t r0 = static_cast<int32_t>((kb - G - a * per_adapter) * 32u);
                             mbar_arrive_expect_tx_cluster(full_even, kTileBytesA + kTileBytesB);
-                            tma_load_2d_pair(sm.a[s], &tmV, full_even, r0, my_m);
+                            tma_load_2d_pair(sm.a[s], &tmV, full_even, 2 * r0, my_m);
                             tma_load_2d_pair(sm.b[s], &tmD, full_even, r0,
                                              __ldg(list + 1 + a) * static_cast<int32_t>(sh.N) + my_n);
                             issued = it + 1;
@@ -313,11 +314,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bool adapter_block = false;
                     if constexpr (kLora) adapter_block = kb >= G;
                     if (adapter_block) {
-                        // 16 of the rank (32 bytes) per MMA; what lies past the rank is zero in both operands
-                        const uint32_t r0 = per_adapter ? (kb - G) % per_adapter * 64u : 0u;
-                        const uint32_t steps = lo.rank - r0 >= 64u ? 4u : (lo.rank - r0 + 15u) / 16u;
-                        for (uint32_t kk = 0; kk < steps; ++kk)
-                            mma_bf16_pair(d, ad + 2u * kk, bd + 2u * kk, idesc_bf16_f32(BM_PAIR, BN), kk > 0 ? 1u : 0u);
+                        // 16 of the rank (32 bytes) per MMA, both parts of v with them; what lies past the
+                        // rank is zero in both operands
+                        const uint32_t r0 = per_adapter ? (kb - G) % per_adapter * 32u : 0u;
+                        const uint32_t steps = lo.rank - r0 >= 32u ? 2u : (lo.rank - r0 + 15u) / 16u;
+                        for (uint32_t kk = 0; kk < steps; ++kk) {
+                            mma_bf16_pair(d, ad + 4u * kk, bd + 2u * kk, idesc_bf16_f32(BM_PAIR, BN), kk > 0 ? 1u : 0u);
+                            mma_bf16_pair(d, ad + 4u * kk + 2u, bd + 2u * kk, idesc_bf16_f32(BM_PAIR, BN), 1u);
+                        }
                     } else {
 #pragma unroll
                         for (uint32_t kk = 0; kk < BK / 32; ++kk)  // K = 32 bytes per MMA: +2 in the address field
@@ -1179,7 +1183,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, cudaStream_t stream) {
     if (!make_map_u8(&ta, L.q, L.k, L.m, BM) || !make_map_u8(&tb, L.wq, L.k, L.n, BN_CTA) ||
         !make_map_scales_box(&ts, L.s_k, L.mp, L.k / BK, BM) || !make_map_out_bf16(&ty, L.y, L.n, L.m))
         return cudaErrorInvalidValue;
-    if (L.lora && (!make_map_bf16(&tv, L.lora->v, L.lora->rank, L.m, BM) ||
+    if (L.lora && (!make_map_bf16(&tv, L.lora->v, v_parts(L.lora->rank), L.m, BM) ||
                    !make_map_bf16(&td, L.lora->b, L.lora->rank, static_cast<uint64_t>(L.lora->adapters) * L.n, BN_CTA)))
         return cudaErrorInvalidValue;
     Shape sh;

@@ -52,10 +52,13 @@ cudaError_t launch_check_division(unsigned long long* counts, cudaStream_t strea
 
 // Low-rank adapters beside the projection (device pointers; see lora.cu).
 constexpr uint32_t kAdapterList = 257;  // per 256 rows: a count, then that many adapters
+// bf16 values of a row of the pair kernel's v: for every 16 of the rank, the last ones
+// padded with zeros, 16 first parts and 16 second ones.
+__host__ __device__ constexpr uint32_t v_parts(uint32_t rank) { return (rank + 15u) / 16u * 32u; }
 struct LoraOperands {
     const int32_t* ids;    // [m]
     const int32_t* lists;  // pair kernel: [ceil(m/256)][kAdapterList]
-    const void* v;         // scaled A_a x of each row [m, rank]: fp32 for the decode kernel, bf16 for the pair kernel
+    const void* v;         // scaled A_a x of each row: fp32 [m, rank] for the decode kernel, bf16 [m, v_parts(rank)] for the pair kernel
     const void* b;         // bf16 [adapters, n, rank]
     uint32_t adapters, rank;
     bool decode;  // the decode kernel, 64 rows at a time, whatever m

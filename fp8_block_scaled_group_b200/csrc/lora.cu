@@ -8,10 +8,14 @@
 // in fp32). The projection's kernels (gemm.cu) then add the second sum to
 // their fp32 accumulators, so the output is rounded once and no pass over y
 // is needed. v is fp32 for the decode kernel, which serves large decode batches
-// with many adapters too, 64 rows at a time; for the pair kernel it is rounded
-// to bf16, the tensor core's operand type: that adds to an output at most half
-// a bf16 step of each term of its second sum, no more than the output's own
-// rounding where the adapter's part is no larger than the whole.
+// with many adapters too, 64 rows at a time. The pair kernel multiplies on the
+// tensor cores, whose operand type is bf16: there v is the sum of two bf16 parts,
+// hi = bf16(v) and lo = bf16(v - hi) (v - hi is exact in fp32), and both are
+// multiplied with B into the same fp32 sum. hi + lo is off by at most 2^-8 of lo,
+// 2^-16 |v|: no more than what summing K >= 128 products in fp32 may be off by
+// ((K + 2) 2^-23 of their magnitudes). One part alone, 2^-8 |v|, reached the
+// outputs where the terms of the second sum cancel: up to ten times the bound
+// (257 rows, K = 256, rank 8).
 //
 // Up to 64 rows (a decode batch, each row with an adapter of its own), unless K is
 // so long that a row does not fit in shared memory: a cluster per row, its CTAs splitting K; bound by reading every used A once.
@@ -351,7 +355,8 @@ __global__ void __launch_bounds__(kTileThreads)
             const float scale = __ldg(scaling + a);
             for (uint32_t i = rank * kTileThreads + tid; i < kTileRows * kSlab / 2; i += split * kTileThreads) {
                 const uint32_t r = i / (kSlab / 2), c = i % (kSlab / 2) * 2u;
-                if (sm.ids[r] != a || slab + c >= sh.rank) continue;
+                // The parts are multiplied 16 at a time; past the rank the sums are zero.
+                if (sm.ids[r] != a || slab + c >= (sh.v_fp32 ? sh.rank : v_parts(sh.rank) / 2u)) continue;
                 float2 n[kTileMaxSplit];
 #pragma unroll
                 for (uint32_t p = 0; p < kTileMaxSplit; ++p) {
@@ -365,11 +370,19 @@ __global__ void __launch_bounds__(kTileThreads)
                     sx += n[p].x;
                     sy += n[p].y;
                 }
-                const size_t at = static_cast<size_t>(row0 + r) * sh.rank + slab + c;
-                if (sh.v_fp32)
-                    *reinterpret_cast<float2*>(static_cast<float*>(v) + at) = make_float2(scale * sx, scale * sy);
-                else
-                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(v) + at) = pack_bf16x2(scale * sx, scale * sy);
+                sx *= scale;
+                sy *= scale;
+                const size_t row = row0 + r;
+                if (sh.v_fp32) {
+                    *reinterpret_cast<float2*>(static_cast<float*>(v) + row * sh.rank + slab + c) = make_float2(sx, sy);
+                } else {
+                    uint16_t* to = static_cast<uint16_t*>(v) + row * v_parts(sh.rank) + (slab + c) / 16u * 32u + c % 16u;
+                    const uint32_t hi = pack_bf16x2(sx, sy);
+                    const float hx = __uint_as_float(hi << 16), hy = __uint_as_float(hi & 0xFFFF0000u);
+                    // what an infinity leaves is nothing, not NaN
+                    *reinterpret_cast<uint32_t*>(to) = hi;
+                    *reinterpret_cast<uint32_t*>(to + 16) = pack_bf16x2(isfinite(hx) ? sx - hx : 0.0f, isfinite(hy) ? sy - hy : 0.0f);
+                }
             }
             cluster_sync_all();  // the parts may be overwritten, or the CTA leave
         }

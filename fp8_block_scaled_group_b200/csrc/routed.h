@@ -98,7 +98,7 @@ cudaError_t launch_moe_combine(const CombineLaunch& L, cudaStream_t stream);
 
 // Quantizes x (codes and K-major scales, as the activation quantizer) and
 // forms v = scaling[a] A_a x of the rows that have an adapter: fp32 for the decode
-// kernel (v_fp32; always for m <= kDecodeMaxTokens), else bf16, and `lists` too.
+// kernel (v_fp32; always for m <= kDecodeMaxTokens), else two bf16 parts, and `lists` too.
 struct LoraPrepLaunch {
     const void* x;
     const int32_t* ids;

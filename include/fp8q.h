@@ -518,8 +518,8 @@ size_t fp8q_lora_linear_workspace_bytes(uint32_t m, uint32_t n, uint32_t k, uint
  * a = adapter_ids[t],
  *   y[t][c] = bf16_rn( <the sum of fp8q_gemm_ex> + sum_r v[t][r] * lora_b[a][c][r] ),
  *   v[t][r] = scaling[a] * sum_k x[t][k] * lora_a[a][r][k],
- * both sums in fp32, the second from the unquantized x. v is kept in fp32 for
- * m <= 64; above it may be rounded to bf16 (the tensor core's operand). A row whose
+ * both sums in fp32, the second from the unquantized x; v is held in 16 bits of
+ * significand at least (fp32, or two bf16 parts for the tensor cores). A row whose
  * id is outside [0, adapters) has no adapter: its result is fp8q_linear_ex's, bit for
  * bit for m <= 64 and m > 256; between, another kernel may run, which groups the same
  * fp32 sum otherwise.
