@@ -371,3 +371,52 @@ def test_moe_layers_in_a_captured_graph():
         torch.cuda.synchronize()
         assert torch.equal(replayed.view(torch.int16), want.view(torch.int16))
     assert api.device_error() == 0
+
+
+# ---------------------------------------------------- a row by itself --
+
+@pytest.mark.parametrize("fmt", ["block", "row"])
+@pytest.mark.parametrize("n,k", [(384, 512), (1280, 4096)])
+def test_rows_have_the_same_bits_in_every_batch(n, k, fmt):
+    """Up to K = 4096 the K blocks are never split (whole tiles idle 32 K blocks at most): a row's sum is then taken in
+    one order, by whichever kernel its batch calls for, the plain projection's prefill kernel among them."""
+    x = ref.activations(400, k, 53, DEV)
+    codes, scale = ref.weights(1, n, k, fmt, 54, DEV)
+    want = api.grouped_linear(x, codes, scale, offsets_of([400]))  # rows on M
+    y, err = ref.product(ref.quantized(x), ref.weight_value(codes[0], scale[0]))
+    ref.assert_close(want, y, err)
+    assert torch.equal(want.view(torch.int16), api.linear(x, codes[0], scale[0]).view(torch.int16)), "plain"
+    for m in (1, 31, 32, 56, 57, 100, 152, 153, 256):  # blocks of 64, of 160, rows on M
+        got = api.grouped_linear(x[:m], codes, scale, offsets_of([m]))
+        assert torch.equal(got.view(torch.int16), want[:m].view(torch.int16)), f"{m} rows"
+    # the same rows as one expert's of three, unevenly, in a plan that calls for another kernel
+    three, ts = codes.repeat(3, 1, 1), scale.repeat(3, *[1] * (scale.dim() - 1))
+    for sizes in ([1, 399, 0], [130, 20, 250], [7, 60, 333]):
+        got = api.grouped_linear(x, three, ts, offsets_of(sizes))
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16)), sizes
+
+
+@pytest.mark.parametrize("rows_per", [3, 100, 300])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_rows_nan_stays_in_its_row(rows_per, value):
+    experts, n, k = 4, 384, 640
+    x = ref.activations(experts * rows_per, k, 57, DEV)
+    codes, scale = ref.weights(experts, n, k, "block", 58, DEV)
+    off = offsets_of([rows_per] * experts)
+    want = api.grouped_linear(x, codes, scale, off)
+    bad = [1, rows_per, 2 * rows_per + 2, experts * rows_per - 1]
+    hurt = x.clone()
+    hurt[bad[0], 3] = hurt[bad[1], 600] = value
+    hurt[bad[2:]] = value
+    got = api.grouped_linear(hurt, codes, scale, off)
+    keep = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    assert torch.equal(want[keep].view(torch.int16), got[keep].view(torch.int16))
+    # and through the whole layer: a token's NaN stays in the token
+    w1, s1 = ref.weights(experts, 512, k, "block", 59, DEV)
+    w2, s2 = ref.weights(experts, k, 256, "block", 60, DEV)
+    ids, p = random_ids(x.shape[0], 2, experts, 61), torch.rand(x.shape[0], 2, device=DEV)
+    a = api.moe_ffn(x, ids, p, w1, s1, w2, s2)
+    b = api.moe_ffn(hurt, ids, p, w1, s1, w2, s2)
+    assert torch.equal(a[keep].view(torch.int16), b[keep].view(torch.int16))
+    assert api.device_error() == 0
