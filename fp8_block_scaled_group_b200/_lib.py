@@ -68,6 +68,7 @@ SIGNATURES = {
     "fp8q_moe_route": (ctypes.c_int, [P, P, P, P, U32, U32, U32, P]),
     "fp8q_grouped_linear_workspace_bytes": (SZ, [U32, U32, U32, U32, U32]),
     "fp8q_grouped_linear": (ctypes.c_int, [P, P, P, P, P, I32, P, P, SZ, U32, U32, U32, U32, U32, P]),
+    "fp8q_diag_stalled_grouped_linear": (ctypes.c_int, [P, P, P, P, P, I32, P, P, SZ, U32, U32, U32, U32, U32, ctypes.c_uint64, P]),
     "fp8q_moe_ffn_workspace_bytes": (SZ, [U32, U32, U32, U32, U32]),
     "fp8q_moe_ffn": (ctypes.c_int, [P, P, P, P, P, P, P, I32, P, P, SZ, U32, U32, U32, U32, U32, P]),
     "fp8q_lora_linear_workspace_bytes": (SZ, [U32, U32, U32, U32, U32]),

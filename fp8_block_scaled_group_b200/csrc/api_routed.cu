@@ -2,6 +2,7 @@
 // launch sequence of each call. Declarations and contracts: include/fp8q.h.
 #include "fp8q.h"
 #include "internal.h"
+#include "ptx.cuh"
 #include "routed.h"
 
 using namespace fp8q;
@@ -134,6 +135,34 @@ fp8q_status check_workspace(const void* workspace, size_t bytes, size_t need) {
     return (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && bytes >= need ? FP8Q_OK : FP8Q_ERR_WORKSPACE;
 }
 
+// fp8q_grouped_linear; `diag_budget` as in GroupedLaunch.
+fp8q_status grouped_linear(const void* x, const int32_t* offsets, const int32_t* rows, const void* wq,
+                           const float* w_scale, int32_t weight_format, void* y, void* workspace,
+                           size_t workspace_bytes, uint32_t tokens, uint32_t total_rows, uint32_t experts,
+                           uint32_t n, uint32_t k, long long diag_budget, void* stream) {
+    if (bad_format(weight_format)) return FP8Q_ERR_ARG;
+    fp8q_status st = check_grouped_sizes(tokens, total_rows, experts, n, k);
+    if (st != FP8Q_OK) return st;
+    if (!rows && tokens != total_rows) return FP8Q_ERR_SHAPE;
+    if (tokens == 0 || total_rows == 0) return FP8Q_OK;
+    if (!x || !offsets || !wq || !w_scale || !y || !workspace) return FP8Q_ERR_NULL;
+    if (!aligned16(x) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(y) || !aligned4(offsets) || !aligned4(rows))
+        return FP8Q_ERR_ALIGN;
+    size_t off[5];
+    grouped_layout(total_rows, experts, k, off);
+    if ((st = check_workspace(workspace, workspace_bytes, off[4])) != FP8Q_OK) return st;
+    if ((st = check_device()) != FP8Q_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    float* s_k = reinterpret_cast<float*>(ws + off[1]);
+    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + off[2]);
+    QuantRowsLaunch quant{x, rows, ws, s_k, counters, tokens, total_rows, k, kGroupedCounters};
+    if ((st = from_cuda(launch_quant_rows(quant, s))) != FP8Q_OK) return st;
+    GroupedLaunch L{ws, s_k, offsets, wq, w_scale, y, reinterpret_cast<float*>(ws + off[3]), counters,
+                    total_rows, experts, n, k, weight_format == FP8Q_WEIGHT_PER_ROW, diag_budget};
+    return from_cuda(launch_grouped(L, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -162,27 +191,18 @@ fp8q_status fp8q_grouped_linear(const void* x, const int32_t* offsets, const int
                                 const float* w_scale, int32_t weight_format, void* y, void* workspace,
                                 size_t workspace_bytes, uint32_t tokens, uint32_t total_rows, uint32_t experts,
                                 uint32_t n, uint32_t k, void* stream) {
-    if (bad_format(weight_format)) return FP8Q_ERR_ARG;
-    fp8q_status st = check_grouped_sizes(tokens, total_rows, experts, n, k);
-    if (st != FP8Q_OK) return st;
-    if (!rows && tokens != total_rows) return FP8Q_ERR_SHAPE;
-    if (tokens == 0 || total_rows == 0) return FP8Q_OK;
-    if (!x || !offsets || !wq || !w_scale || !y || !workspace) return FP8Q_ERR_NULL;
-    if (!aligned16(x) || !aligned16(wq) || !aligned16(w_scale) || !aligned16(y) || !aligned4(offsets) || !aligned4(rows))
-        return FP8Q_ERR_ALIGN;
-    size_t off[5];
-    grouped_layout(total_rows, experts, k, off);
-    if ((st = check_workspace(workspace, workspace_bytes, off[4])) != FP8Q_OK) return st;
-    if ((st = check_device()) != FP8Q_OK) return st;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    float* s_k = reinterpret_cast<float*>(ws + off[1]);
-    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + off[2]);
-    QuantRowsLaunch quant{x, rows, ws, s_k, counters, tokens, total_rows, k, kGroupedCounters};
-    if ((st = from_cuda(launch_quant_rows(quant, s))) != FP8Q_OK) return st;
-    GroupedLaunch L{ws, s_k, offsets, wq, w_scale, y, reinterpret_cast<float*>(ws + off[3]), counters,
-                    total_rows, experts, n, k, weight_format == FP8Q_WEIGHT_PER_ROW};
-    return from_cuda(launch_grouped(L, s));
+    return grouped_linear(x, offsets, rows, wq, w_scale, weight_format, y, workspace, workspace_bytes, tokens, total_rows,
+                          experts, n, k, 0, stream);
+}
+
+fp8q_status fp8q_diag_stalled_grouped_linear(const void* x, const int32_t* offsets, const int32_t* rows, const void* wq,
+                                             const float* w_scale, int32_t weight_format, void* y, void* workspace,
+                                             size_t workspace_bytes, uint32_t tokens, uint32_t total_rows,
+                                             uint32_t experts, uint32_t n, uint32_t k, uint64_t wait_budget_cycles,
+                                             void* stream) {
+    if (wait_budget_cycles == 0 || wait_budget_cycles > static_cast<uint64_t>(kWaitBudgetCycles)) return FP8Q_ERR_ARG;
+    return grouped_linear(x, offsets, rows, wq, w_scale, weight_format, y, workspace, workspace_bytes, tokens, total_rows,
+                          experts, n, k, static_cast<long long>(wait_budget_cycles), stream);
 }
 
 size_t fp8q_moe_ffn_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t experts, uint32_t d, uint32_t i) {

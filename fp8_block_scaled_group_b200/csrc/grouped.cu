@@ -252,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         regs_dec<kRegsLow>();
         TokensWalk walk(sm.experts, sh, pair, num_pairs);
         Piece w;
-        if (warp == 0) {
+        if (warp == 0 && !sh.no_copies) {
             auto weight_row = [&](const Piece& p) {
                 return static_cast<int32_t>(p.expert * sh.N + (p.n0 + rank * BW < sh.N ? p.n0 + rank * BW : p.n0));
             };
@@ -296,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     issued = it + 1;
                 }
             }
-        } else if (warp < 3 && rank == 0) {
+        } else if ((warp == 1 || warp == 2) && rank == 0) {
             // Two MMA issuers, by K-block parity, as in the plain projection.
             const uint32_t par = warp - 1u;
             uint32_t it = 0;
@@ -557,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         regs_dec<kRegsLow>();
         RowsWalk walk(sm.experts, sh, pair, num_pairs);
         Piece w;
-        if (warp == 0) {
+        if (warp == 0 && !sh.no_copies) {
             uint32_t it = 0;
             bool ok = true;
             while (ok && walk.pop(w)) {
@@ -964,7 +964,8 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t stream) {
     sh.num_n = (L.n + BW_PAIR - 1) / BW_PAIR;
     sh.total_pad = pad;
     sh.w_per_row = L.w_per_row ? 1u : 0u;
-    sh.budget = kWaitBudgetCycles;
+    sh.no_copies = L.diag_budget != 0 ? 1u : 0u;
+    sh.budget = L.diag_budget != 0 ? L.diag_budget : kWaitBudgetCycles;
     CUtensorMap tw, tt, tx;  // weights, rows, and the scales (tokens kernel) or the output (rows kernel)
     if (!make_map(&tw, L.wq, L.k, static_cast<uint64_t>(L.experts) * L.n, few ? BW : BN_CTA / 2) ||
         !make_map(&tt, L.q, L.k, L.total, few ? 16u : BM) ||

@@ -22,7 +22,8 @@ struct GroupedShape {
     uint32_t num_n;      // 256-column weight tiles per expert
     uint32_t total_pad;  // row extent of the K-major scales
     uint32_t w_per_row;
-    long long budget;
+    uint32_t no_copies;  // timeout diagnostics: the producer issues no copies
+    long long budget;    // clock budget of every wait
 };
 
 // The groups, in shared memory.

@@ -49,6 +49,9 @@ struct GroupedLaunch {
     uint32_t* counters;      // kGroupedCounters words, zero
     uint32_t total, experts, n, k;
     bool w_per_row;
+    // Timeout diagnostics only (0 in normal use): the kernel's producer
+    // issues no copies and each wait is bounded by this many clocks.
+    long long diag_budget = 0;
 };
 
 // Split-K bookkeeping of one grouped projection.

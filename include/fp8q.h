@@ -619,6 +619,20 @@ fp8q_status fp8q_diag_stalled_linear(const void *x, const void *wq, const float 
                                      uint32_t m, uint32_t n, uint32_t k,
                                      uint64_t wait_budget_cycles, void *stream);
 
+/*
+ * The same for fp8q_grouped_linear: its quantizer runs, then the projection that
+ * the sizes select stalls (its copies suppressed) and raises bit 3 of the error
+ * word. Device error, y and workspace as above; a projection without a group of
+ * any row has nothing to wait for and raises nothing.
+ * Errors: ARG, and those of fp8q_grouped_linear.
+ */
+fp8q_status fp8q_diag_stalled_grouped_linear(const void *x, const int32_t *offsets, const int32_t *rows,
+                                             const void *wq, const float *w_scale, int32_t weight_format,
+                                             void *y, void *workspace, size_t workspace_bytes,
+                                             uint32_t tokens, uint32_t total_rows, uint32_t experts,
+                                             uint32_t n, uint32_t k, uint64_t wait_budget_cycles,
+                                             void *stream);
+
 /* Number of kernels this library has launched in this process. */
 uint64_t fp8q_launch_count(void);
 

@@ -151,3 +151,19 @@ def test_python_refuses_what_is_not_on_a_device():
         api.lora_linear(x, w[0], s[0], torch.zeros(3, dtype=torch.int32), x[None, :, :128], torch.zeros(1, 128, 3, dtype=torch.bfloat16), torch.ones(1))
     with pytest.raises(ValueError, match="wq 3-D"):
         api.grouped_linear(x, w[0], s, torch.zeros(3, dtype=torch.int32))
+
+
+def test_stalled_grouped_linear_refuses_what_the_call_refuses():
+    lib, args = _lib.load(), dict(DEFAULTS["fp8q_grouped_linear"])
+
+    def stalled(budget, **change):
+        a = {**args, **change}
+        stream = a.pop("stream")
+        return lib.fp8q_diag_stalled_grouped_linear(*a.values(), budget, stream)
+
+    assert stalled(0) == ARG and stalled(2_000_000_001) == ARG  # no budget, and past the second that a wait lasts at most
+    assert stalled(1000, fmt=2) == ARG and stalled(1000, n=100) == SHAPE and stalled(1000, rows=None) == SHAPE
+    assert stalled(1000, x=None) == NULL and stalled(1000, y=BASE + 8) == ALIGN and stalled(1000, bytes=1000) == WORKSPACE
+    assert stalled(1000, tokens=0) == OK
+    if not torch.cuda.is_available():
+        assert stalled(1000) in (CUDA, UNSUPPORTED)
