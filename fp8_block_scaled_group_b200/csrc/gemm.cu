@@ -1080,7 +1080,11 @@ cudaError_t read_clear_device_error(uint32_t* code, cudaStream_t stream) {
     return e;
 }
 
-// Once per device ordinal: the attribute is the device's.
+namespace {
+
+// Once per device ordinal: the attribute is the device's. In this namespace, because
+// what a template keeps would otherwise be shared by all copies of the library in a
+// process.
 template <uint32_t NT, bool FUSE, bool LORA>
 cudaError_t decode_smem_optin() {
     static std::once_flag once[64];
@@ -1166,6 +1170,8 @@ cudaError_t launch_decode(const GemmLaunch& L, int sms, cudaStream_t stream) {
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t launch_gemm(const GemmLaunch& L, cudaStream_t stream) {
     const KernelSetup& ks = setup_for_device();

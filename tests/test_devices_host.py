@@ -9,6 +9,7 @@ intermediate form only, which nothing loads.
 import ctypes
 import glob
 import os
+import shutil
 import subprocess
 
 import pytest
@@ -21,8 +22,15 @@ BASE = (ctypes.addressof(BUF) + 255) // 256 * 256  # aligned; never read: nothin
 BIG = 1 << 40
 
 
+def declare(lib):
+    for name, (restype, argtypes) in _lib.SIGNATURES.items():
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, argtypes
+    return lib
+
+
 @pytest.fixture(scope="module")
-def lib(tmp_path_factory):
+def library(tmp_path_factory):
     out = tmp_path_factory.mktemp("devices")
     so = str(out / "libfp8q_checked.so")
     cuda = os.path.dirname(os.path.dirname(build.nvcc()))
@@ -31,11 +39,12 @@ def lib(tmp_path_factory):
     subprocess.check_call([build.nvcc(), "-t", "0", "-gencode", "arch=compute_100a,code=compute_100a", "-std=c++17", "-cudart", "none",
                            "-shared", "-Xcompiler", "-fPIC,-O1", "-Xlinker", "-Bsymbolic", "-I", build.INCLUDE, "-I", build.CSRC, *build.sources(),
                            str(out / "fake.o"), "-o", so])
-    lib = ctypes.CDLL(so)
-    for name, (restype, argtypes) in _lib.SIGNATURES.items():
-        fn = getattr(lib, name)
-        fn.restype, fn.argtypes = restype, argtypes
-    return lib
+    return so
+
+
+@pytest.fixture(scope="module")
+def lib(library):
+    return declare(ctypes.CDLL(library))
 
 
 N, K, E = 384, 1152, 8
@@ -63,3 +72,16 @@ def test_each_device_is_prepared(lib, what):
         before, refused = lib.fake_launches(device), lib.fake_refused()
         assert getattr(lib, name)(*args, None) == 0, f"{what} on device {device}"
         assert lib.fake_launches(device) > before and lib.fake_refused() == refused
+
+
+def test_two_copies_of_the_library_in_one_process(lib, library, tmp_path):
+    """A copy that another package brings along has kernels of its own, which it has to prepare itself whatever the first
+    one has done: no state of one is the other's."""
+    for name, args in CALLS.values():
+        assert getattr(lib, name)(*args, None) == 0
+    second = str(tmp_path / "libfp8q_second.so")
+    shutil.copy(library, second)
+    other = declare(ctypes.CDLL(second))
+    for what, (name, args) in CALLS.items():
+        assert getattr(other, name)(*args, None) == 0, what
+    assert other.fake_refused() == 0
