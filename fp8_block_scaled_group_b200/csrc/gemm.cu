@@ -315,7 +315,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if constexpr (kLora) adapter_block = kb >= G;
                     if (adapter_block) {
                         // 16 of the rank (32 bytes) per MMA, both parts of v with them; what lies past the
-                        // rank is zero in both operands
+                        // rank is zero in both operands. A count known at compile time (two steps always)
+                        // changes how the whole kernel is compiled: 204 us instead of 183 (4576 rows,
+                        // 6144 x 6144, rank 16).
                         const uint32_t r0 = per_adapter ? (kb - G) % per_adapter * 32u : 0u;
                         const uint32_t steps = lo.rank - r0 >= 32u ? 2u : (lo.rank - r0 + 15u) / 16u;
                         for (uint32_t kk = 0; kk < steps; ++kk) {

@@ -428,8 +428,8 @@ fp8q_status fp8q_dequant_fp8_bf16(const void *wq, const float *w_scale, int32_t 
  * arithmetic of a row is the plain projection's (fp8q_quant_act, then
  * fp8q_gemm_ex): a row's result does not depend on the rows beside it except
  * for the last bits of the fp32 sum when few tiles make the K blocks be split
- * (the split depends on all groups' sizes). The same inputs always give the
- * same bits.
+ * (never up to k = 4096; the split depends on all groups' sizes). The same inputs
+ * always give the same bits. A NaN or infinity in a row of x reaches no other row.
  *
  * Device data that the host cannot check (ids, offsets, rows) never causes
  * an access out of bounds: ids outside [0, experts) drop the slot, offsets are
@@ -458,9 +458,9 @@ size_t fp8q_grouped_linear_workspace_bytes(uint32_t tokens, uint32_t total_rows,
                                            uint32_t n, uint32_t k);
 
 /*
- * FP8 projection grouped by expert, ragged groups: x is quantized once, and
- * for every group e and grouped row i in it, with r = rows[i] (or i when rows
- * is NULL),
+ * FP8 projection grouped by expert, ragged groups: row r of x is quantized once
+ * for every grouped row that names it, and for every group e and grouped row i in
+ * it, with r = rows[i] (or i when rows is NULL),
  *   y[i][c] = bf16_rn( sum_g s[r][g] * ws_e(c, g) * sum_{j<128} q[r][128g+j] * wq[e][c][128g+j] ).
  *   x        bf16 [tokens, k]                                     (input)
  *   offsets  int32 [experts + 1], device memory                   (input)
