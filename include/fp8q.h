@@ -492,7 +492,8 @@ size_t fp8q_moe_ffn_workspace_bytes(uint32_t tokens, uint32_t topk, uint32_t exp
  *   q_h, s_h  = fp8q_silu_mul_quant(gate, up)
  *   s         = grouped projection of q_h        (bf16)
  *   y[t]      = bf16_rn( sum_j topk_weights[t][j] * s[pos[t][j]] )   (fp32, j ascending)
- * Dropped slots add nothing; a token whose slots are all dropped gives zeros.
+ * Dropped slots add nothing; a token whose slots are all dropped gives zeros. y may
+ * be x.
  *   x bf16 [tokens, d]; topk_ids int32, topk_weights fp32 [tokens, topk]
  *   w_gate_up e4m3 [experts, 2i, d] (gate rows first), w_down e4m3 [experts, d, i],
  *   scales in `weight_format` for both; y bf16 [tokens, d]

@@ -420,3 +420,45 @@ def test_a_rows_nan_stays_in_its_row(rows_per, value):
     b = api.moe_ffn(hurt, ids, p, w1, s1, w2, s2)
     assert torch.equal(a[keep].view(torch.int16), b[keep].view(torch.int16))
     assert api.device_error() == 0
+
+
+def test_many_rows():
+    """More rows than a grid's second axis could count, groups of half a million of them."""
+    sizes = [1 << 19, 0, 1, (1 << 19) - 77]
+    x = ref.activations(sum(sizes), 128, 62, DEV)
+    codes, scale = ref.weights(len(sizes), 128, 128, "block", 63, DEV)
+    check_grouped(x, codes, scale, offsets_of(sizes), None)
+    check_moe(70001, 2, 5, 128, 128, "block", 0.1, 64)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured layers of other sizes with one workspace, replayed in turn: neither finds anything of the other's."""
+    parts = []
+    need = 0
+    for t, topk, experts, d, i, seed in ((9, 4, 16, 512, 256, 70), (300, 2, 3, 17408, 128, 71)):
+        (w1, s1), (w2, s2) = ref.weights(experts, 2 * i, d, "block", seed, DEV), ref.weights(experts, d, i, "block", seed + 5, DEV)
+        x, ids, p = ref.activations(t, d, seed, DEV), random_ids(t, topk, experts, seed, 0.2), torch.rand(t, topk, device=DEV)
+        parts.append([x, ids, p, w1, s1, w2, s2])
+        need = max(need, api.moe_ffn_workspace_bytes(t, topk, experts, d, i))
+    work = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want = [api.moe_ffn(*a) for a in parts]
+    graphs, outs = [], [torch.empty_like(w) for w in want]
+    for a, out in zip(parts, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            api.moe_ffn(*a, workspace=work, out=out)
+    for turn in (0, 1, 1, 0, 1, 0, 0):
+        outs[turn].zero_()
+        graphs[turn].replay()
+        assert torch.equal(outs[turn].view(torch.int16), want[turn].view(torch.int16))
+    assert api.device_error() == 0
+
+
+def test_layer_in_place():
+    """The layer reads x before it writes y: the output may take the input's place."""
+    t, topk, experts, d, i = 150, 3, 6, 384, 256
+    (w1, s1), (w2, s2) = ref.weights(experts, 2 * i, d, "block", 76, DEV), ref.weights(experts, d, i, "block", 77, DEV)
+    x, ids, p = ref.activations(t, d, 78, DEV), random_ids(t, topk, experts, 79, 0.1), torch.rand(t, topk, device=DEV)
+    want = api.moe_ffn(x, ids, p, w1, s1, w2, s2)
+    api.moe_ffn(x, ids, p, w1, s1, w2, s2, out=x)
+    assert torch.equal(x.view(torch.int16), want.view(torch.int16))
